@@ -307,13 +307,15 @@ template <typename T, bool kEntropy, int kN, int kStride> struct Acc {
     s += sc;
     u += uc;
   }
-  // The reference becomes the largest of the lanes' t.
+  // The reference becomes the largest of the lanes' t. In the fast form the sums are relative to R, which is off
+  // from m c by rest(), up to 2^-9; in the slow one to m c itself.
   __device__ __forceinline__ void move(float t, float c) {
-    const float m = warp_max(t), old = ref.m, oldR = ref.R;
-    const bool was_slow = ref.slow;
+    const float m = warp_max(t);
+    const Ref old = ref;
     ref.set(m, c);
     if (set) {
-      const float d = was_slow || ref.slow ? fmaxf((old - m) * c, -1e4f) : oldR - ref.R, f = ex2(d);
+      const float d = old.slow || ref.slow ? fmaxf((old.m - m) * c - old.rest(c) + ref.rest(c), -1e4f) : old.R - ref.R;
+      const float f = ex2(d);
       u = (u + d * s) * f;
       s *= f;
     }
