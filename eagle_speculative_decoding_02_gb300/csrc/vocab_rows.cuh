@@ -158,6 +158,10 @@ __device__ __forceinline__ Two in_temperatures(Two d, const Scale& c) {  // d / 
   x.l += d.h * c.inv_lo;
   return x;
 }
+// (z - top) / temperature where the difference is beyond float32's range, which the division may bring back.
+inline __device__ __noinline__ double far_in_temperatures(float z, float top, const Scale& c) {
+  return ((double)z - top) * ((double)c.inv + c.inv_lo);
+}
 __device__ __forceinline__ Two warp_sum_two(Two v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = v + Two{__shfl_xor_sync(kFull, v.h, o), __shfl_xor_sync(kFull, v.l, o)};
@@ -573,7 +577,9 @@ struct Answer {
     log_s = log_of(all);
   }
   __device__ float logprob(float z, const Scale& c) const {
-    return (in_temperatures(sum_of(z, -top), c) - log_s).value();
+    const Two away = sum_of(z, -top);
+    if (away.h == -INFINITY && z != -INFINITY) return far_in_temperatures(z, top, c);  // log_s is below its last bit
+    return (in_temperatures(away, c) - log_s).value();
   }
 };
 
@@ -766,7 +772,7 @@ __device__ __forceinline__ void store_loss(const Distill& d, int64_t row, const 
     if (t.p[i] > 0.f && t.idx[i] >= 0) {
       const Two away = sum_of(t.z[i], -s.top);
       if (away.h == -INFINITY && t.z[i] != -INFINITY)  // beyond float's range, but a small p may bring it back
-        loss = loss + Two{(float)(((double)s.top - t.z[i]) * ((double)c.inv + c.inv_lo) * t.p[i]), 0.f};
+        loss = loss + Two{(float)(-far_in_temperatures(t.z[i], s.top, c) * t.p[i]), 0.f};
       else
         loss = loss + (Two{t.lp[i], 0.f} - (in_temperatures(away, c) - log_s)) * t.p[i];
     }
