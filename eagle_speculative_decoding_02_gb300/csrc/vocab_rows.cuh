@@ -770,11 +770,11 @@ __device__ __forceinline__ void store_loss(const Distill& d, int64_t row, const 
   for (int h = 0; h < 2; ++h) {
     const int i = lane + 32 * h;
     if (t.p[i] > 0.f && t.idx[i] >= 0) {
-      const Two away = sum_of(t.z[i], -s.top);
+      const Two away = in_temperatures(sum_of(t.z[i], -s.top), c);
       if (away.h == -INFINITY && t.z[i] != -INFINITY)  // beyond float's range, but a small p may bring it back
         loss = loss + Two{(float)(-far_in_temperatures(t.z[i], s.top, c) * t.p[i]), 0.f};
       else
-        loss = loss + (Two{t.lp[i], 0.f} - (in_temperatures(away, c) - log_s)) * t.p[i];
+        loss = loss + (Two{t.lp[i], 0.f} - (away - log_s)) * t.p[i];
     }
   }
   loss = warp_sum_two(loss);
