@@ -380,6 +380,9 @@ __device__ void scan_rows(Smem<kLogprobs>& sm, const Args& a, int rank, int wid,
         const uint32_t slot = g % kSlots, turn = g / kSlots;
         ++seen;
         if (g++ % kScan != wid) return;
+        // The slot's turn before was another warp's. While its copy has not landed, the parity to wait for is that of
+        // the turn before it, which has: so first the end of that turn (the one before was over when it was asked for).
+        if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1, ab);
         wait(&sm.full[slot], turn & 1, ab);
         const uint4* chunk = sm.ring[slot];
         if (first) {
