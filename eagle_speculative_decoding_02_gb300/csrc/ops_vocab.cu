@@ -107,4 +107,9 @@ eagle_status eagle_op_distill_loss_grad(int32_t dtype, int32_t rows, int32_t voc
   return launched([&] { return distill_loss_grad(r, d, (cudaStream_t)stream); });
 }
 
+eagle_status eagle_selftest_vocab_wait(int64_t ns) {
+  set_vocab_wait(ns);
+  return EAGLE_OK;
+}
+
 }  // extern "C"

@@ -76,8 +76,13 @@ template <int kMode> struct Shape {
 
 // ---- barriers --------------------------------------------------------------------------------------
 
-// Waits end after 2 s at the latest (tc::kTimeoutNs): the block then gives up, every
-// later wait of it returns at once, and the call's results are incomplete.
+// A wait ends after Args::wait_ns at the latest (2 s). The block then gives up: every later wait of it that is not
+// over already fails at once, each role leaves its rows at a wait that failed, before it uses what it waited for, and
+// the results of all the cluster's rows become NaN (give_up). The cluster's other blocks miss its parts and follow.
+struct Limit {
+  unsigned long long ns;
+  int over;
+};
 template <bool kCluster> __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
   if (!kCluster) return tc::mbar_try_wait(bar, parity);
   uint32_t ok;
@@ -87,21 +92,43 @@ template <bool kCluster> __device__ __forceinline__ bool try_wait(uint64_t* bar,
       : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(tc::kSuspendNs) : "memory");
   return ok != 0;
 }
-template <bool kCluster> __device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool time_is_up(uint32_t tries, unsigned long long t0, const Limit* limit) {
+  return limit->ns == 0 || (tries % 64 == 63 && tc::globaltimer() - t0 > limit->ns);
+}
+// One thread.
+__device__ __noinline__ bool wait_one(uint64_t* bar, uint32_t parity, Limit* limit) {
   const unsigned long long t0 = tc::globaltimer();
-  for (uint32_t i = 1; !try_wait<kCluster>(bar, parity); ++i) {
-    if (*abort_flag) return;
-    if ((i & 63) == 0 && tc::globaltimer() - t0 > tc::kTimeoutNs) *abort_flag = 1;
+  for (uint32_t i = 0; !try_wait<false>(bar, parity); ++i) {
+    if (time_is_up(i, t0, limit)) *(volatile int*)&limit->over = 1;
+    if (*(volatile int*)&limit->over) return false;
   }
+  return true;
+}
+// A warp: the same answer for all its lanes.
+template <bool kCluster> __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, Limit* limit) {
+  const unsigned long long t0 = tc::globaltimer();
+#pragma unroll 1
+  for (uint32_t i = 0; !__all_sync(kFull, try_wait<kCluster>(bar, parity)); ++i) {
+    const bool over = *(volatile int*)&limit->over || time_is_up(i, t0, limit);
+    if (__any_sync(kFull, over)) {
+      *(volatile int*)&limit->over = 1;
+      return false;
+    }
+  }
+  return true;
 }
 template <bool kCluster = false>
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (!try_wait<kCluster>(bar, parity)) wait_long<kCluster>(bar, parity, abort_flag);
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Limit* limit) {
+  return __all_sync(kFull, try_wait<kCluster>(bar, parity)) || wait_long<kCluster>(bar, parity, limit);
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
+}
+// The cluster's rows: the first, and the distance to the next.
+__device__ __forceinline__ void cluster_rows(uint32_t& row0, uint32_t& step) {
+  asm volatile("mov.u32 %0, %%clusterid.x;\nmov.u32 %1, %%nclusterid.x;" : "=r"(row0), "=r"(step));
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
@@ -141,11 +168,13 @@ template <typename T> struct Part : Row<T> {
     unit = a.unit;
   }
   __device__ int begin(int u) const { return min(this->nb, u * unit); }  // of unit u
-  // f(first vector, vectors) for each chunk of unit u
-  template <int kChunk, typename F> __device__ __forceinline__ void chunks(int u, F f) const {
+  // f(first vector, vectors) for each chunk of unit u, until one is false
+  template <int kChunk, typename F> __device__ __forceinline__ bool chunks(int u, F f) const {
     const int e = begin(u + 1);
 #pragma unroll 1
-    for (int v = begin(u); v < e; v += kChunk) f(v, min(kChunk, e - v));
+    for (int v = begin(u); v < e; v += kChunk)
+      if (!f(v, min(kChunk, e - v))) return false;
+    return true;
   }
 };
 
@@ -192,7 +221,8 @@ template <int kMode> struct Smem {
   uint64_t done[kBuf];          // the row is done with
   uint64_t scanned[2], taken[2];    // a row's candidates are there, are done with
   uint64_t listed, unlisted;        // the block's list is there, is done with
-  int abort_flag;
+  Limit limit;
+  uint32_t copied;  // chunks that the copying warp asked for
 };
 // Where row number `it` of a block keeps its data, and the parity of that place's barriers.
 template <int kMode> __device__ __forceinline__ int buf_of(int it) { return it % Shape<kMode>::kBuf; }
@@ -209,21 +239,40 @@ __device__ void copy_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0
     const Part<T> z(a, row, rank);
 #pragma unroll 1
     for (int u = z.u0; u < z.u1; ++u)
-      z.template chunks<Shape<kMode>::kChunk>(u, [&](int v, int n) {
-        const uint32_t slot = g % kSlots, turn = g / kSlots;
-        if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1, &sm.abort_flag);
-        if (*(volatile int*)&sm.abort_flag) return;
-        tc::mbar_expect_tx(&sm.full[slot], n * 16);
-        tc::bulk_load(sm.ring[slot], z.row + z.entry(v), n * 16, &sm.full[slot]);
-        ++g;
-      });
+      if (!z.template chunks<Shape<kMode>::kChunk>(u, [&](int v, int n) {
+            const uint32_t slot = g % kSlots, turn = g / kSlots;
+            if (turn > 0 && !wait_one(&sm.empty[slot], (turn - 1) & 1, &sm.limit)) return false;
+            tc::mbar_expect_tx(&sm.full[slot], n * 16);
+            tc::bulk_load(sm.ring[slot], z.row + z.entry(v), n * 16, &sm.full[slot]);
+            ++g;
+            return true;
+          })) {
+        sm.copied = g;
+        return;
+      }
   }
-  // what is in flight has to land before the block ends (only a block that gave up leaves copies unread)
-  if (*(volatile int*)&sm.abort_flag)
+  sm.copied = g;
+}
+
+// After the roles of a block that gave up (all of the cluster's have ended): what is under way to its shared memory
+// has to land before it ends, and nobody may take what stands in the rows' results for such.
+template <typename T, int kMode> __device__ __noinline__ void give_up(Smem<kMode>& sm, const Args& a) {
+  if (threadIdx.x == 0) {
+    // copies, by the chunks' barriers, 0.2 s each at most
+    const uint32_t g = sm.copied;
 #pragma unroll 1
     for (uint32_t o = g > kSlots ? g - kSlots : 0; o < g; ++o)
+#pragma unroll 1
       for (int tries = 0; tries < 100000 && !try_wait<false>(&sm.full[o % kSlots], (o / kSlots) & 1); ++tries) {
       }
+    // sums that other blocks sent, of which nothing here tells how many: they take microseconds, this a millisecond
+#pragma unroll 1
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  uint32_t row0, step;
+  cluster_rows(row0, step);
+#pragma unroll 1
+  for (int64_t row = row0; row < a.r.rows; row += step) no_results<T, kMode>(a, row, threadIdx.x, blockDim.x);
 }
 
 // ---- summing warps ---------------------------------------------------------------------------------
@@ -234,12 +283,12 @@ __device__ void sum_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0,
   constexpr int kVec = El<T>::kVec;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = a.c.hi;
-  volatile int* ab = &sm.abort_flag;
+  Limit* limit = &sm.limit;
   uint32_t g = 0;
   // a row's sums; the slots stay taken in a step
   auto sum = [&](int64_t row, int it) {
     const int b = buf_of<kMode>(it);
-    wait(&sm.ready[b], turn_of<kMode>(it), ab);
+    if (!wait(&sm.ready[b], turn_of<kMode>(it), limit)) return false;
     Acc<T, kMode == kLogprobs, kPer, S::kNT> acc;
     acc.clear();
     if constexpr (kMode == kLogprobs) {
@@ -247,14 +296,16 @@ __device__ void sum_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0,
 #pragma unroll 1
       for (int u = z.u0; u < z.u1; ++u) {
         if (u > z.u0) acc.clear();
-        z.template chunks<S::kChunk>(u, [&](int, int n) {
-          const uint32_t slot = g % kSlots;
-          wait(&sm.full[slot], (g / kSlots) & 1, ab);
-          acc.add(sm.ring[slot], tid, n, c);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.empty[slot]);
-          ++g;
-        });
+        if (!z.template chunks<S::kChunk>(u, [&](int, int n) {
+              const uint32_t slot = g % kSlots;
+              if (!wait(&sm.full[slot], (g / kSlots) & 1, limit)) return false;
+              acc.add(sm.ring[slot], tid, n, c);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.empty[slot]);
+              ++g;
+              return true;
+            }))
+          return false;
         const Sums w = acc.total(c);
         if (lane == 0) sm.warp[b][u - z.u0][warp] = w;
       }
@@ -265,7 +316,7 @@ __device__ void sum_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0,
 #pragma unroll 1
       for (int left = x.n_vec; left > 0; left -= S::kChunk, me += S::kNW, ++g) {
         const uint32_t slot = g % kSlots;
-        wait(&sm.full[slot], (g / kSlots) & 1, ab);
+        if (!wait(&sm.full[slot], (g / kSlots) & 1, limit)) return false;
         // The listed entries become -inf: the sums are those of the unlisted. (Taking them off the full sum
         // instead would leave nothing of an unlisted share below 2^-24.)
 #pragma unroll
@@ -285,12 +336,13 @@ __device__ void sum_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0,
       if (lane == 0) sm.warp[b][0][warp] = w;
     }
     if (lane == 0) mbar_arrive(&sm.sums[b]);
+    return true;
   };
   // a row's gradient; `slots` counts its chunks
   auto grad = [&](int it, uint32_t& slots) {
     if constexpr (kMode == kStep || kMode == kGrad) {
       const int b = buf_of<kMode>(it);
-      wait(kMode == kStep ? &sm.joined[b] : &sm.ready[b], turn_of<kMode>(it), ab);
+      if (!wait(kMode == kStep ? &sm.joined[b] : &sm.ready[b], turn_of<kMode>(it), limit)) return false;
       const DistillRow& x = sm.x[b];
       const int owner[2] = {x.owner[lane], x.owner[lane + 32]}, at[2] = {x.at[lane], x.at[lane + 32]};
       const Ref ref = x.k.ref;
@@ -301,7 +353,7 @@ __device__ void sum_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0,
 #pragma unroll 1
       for (int left = x.n_vec; left > 0; left -= S::kChunk, me += S::kNW, ++slots, out += S::kChunk * kVec) {
         const uint32_t slot = slots % kSlots;
-        if (kMode == kGrad) wait(&sm.full[slot], (slots / kSlots) & 1, ab);
+        if (kMode == kGrad && !wait(&sm.full[slot], (slots / kSlots) & 1, limit)) return false;
         const uint4* in = sm.ring[slot];
         if (aligned && left >= S::kChunk) {  // without a branch per vector
 #pragma unroll
@@ -326,21 +378,21 @@ __device__ void sum_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0,
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.done[b]);
     }
+    return true;
   };
   if constexpr (kMode == kStep) {
     uint32_t written = 0;
     int it = 0;
 #pragma unroll 1
     for (int64_t row = row0; row < a.r.rows + step; row += step, ++it) {
-      if (row < a.r.rows) sum(row, it);
-      if (it > 0) grad(it - 1, written);
+      if (row < a.r.rows && !sum(row, it)) return;
+      if (it > 0 && !grad(it - 1, written)) return;
     }
   } else {
     int it = 0;
 #pragma unroll 1
     for (int64_t row = row0; row < a.r.rows; row += step, ++it) {
-      if constexpr (kMode == kGrad) grad(it, g);
-      else sum(row, it);
+      if (kMode == kGrad ? !grad(it, g) : !sum(row, it)) return;
     }
   }
 }
@@ -361,7 +413,7 @@ __device__ void scan_rows(Smem<kLogprobs>& sm, const Args& a, int rank, int wid,
   static_assert(kAtOnce * kRounds <= 32, "a bit a vector");
   const int lane = threadIdx.x & 31, k = a.t.k;
   const uint32_t below = (1u << lane) - 1;
-  volatile int* ab = &sm.abort_flag;
+  Limit* limit = &sm.limit;
   ScanSmem& x = sm.x;
   uint32_t g = 0;
   int it = 0;
@@ -371,54 +423,56 @@ __device__ void scan_rows(Smem<kLogprobs>& sm, const Args& a, int rank, int wid,
     const Part<T> z(a, row, rank);
     unsigned long long* cand = x.cand[b][wid];
     Cut* cut = &x.cut[b];
-    if (it >= 2) wait(&sm.taken[b], ph ^ 1, ab);
+    if (it >= 2 && !wait(&sm.taken[b], ph ^ 1, limit)) return;
     int seen = 0, n_cand = 0;
     bool first = true;
 #pragma unroll 1
     for (int u = z.u0; u < z.u1; ++u)
-      z.template chunks<S::kChunk>(u, [&](int v0, int n) {
-        const uint32_t slot = g % kSlots, turn = g / kSlots;
-        ++seen;
-        if (g++ % kScan != wid) return;
-        // The slot's turn before was another warp's. While its copy has not landed, the parity to wait for is that of
-        // the turn before it, which has: so first the end of that turn (the one before was over when it was asked for).
-        if (turn > 0) wait(&sm.empty[slot], (turn - 1) & 1, ab);
-        wait(&sm.full[slot], turn & 1, ab);
-        const uint4* chunk = sm.ring[slot];
-        if (first) {
-          first = false;
-          float most[kAtOnce];
+      if (!z.template chunks<S::kChunk>(u, [&](int v0, int n) {
+            const uint32_t slot = g % kSlots, turn = g / kSlots;
+            ++seen;
+            if (g++ % kScan != wid) return true;
+            // The slot's turn before was another warp's. While its copy has not landed, the parity to wait for is that of
+            // the turn before it, which has: so first the end of that turn (the one before was over when it was asked for).
+            if (turn > 0 && !wait(&sm.empty[slot], (turn - 1) & 1, limit)) return false;
+            if (!wait(&sm.full[slot], turn & 1, limit)) return false;
+            const uint4* chunk = sm.ring[slot];
+            if (first) {
+              first = false;
+              float most[kAtOnce];
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) most[i] = -INFINITY;
+              for (int i = 0; i < kAtOnce; ++i) most[i] = -INFINITY;
 #pragma unroll 1
-          for (int r = 0; r < kRounds; ++r)
+              for (int r = 0; r < kRounds; ++r)
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-              const int v = (r * kAtOnce + i) * 32 + lane;
-              const float t = vec_max<T>(chunk[min(v, n - 1)]);
-              if (v < n) most[i] = fmaxf(most[i], t);  // each entry once only
+                for (int i = 0; i < kAtOnce; ++i) {
+                  const int v = (r * kAtOnce + i) * 32 + lane;
+                  const float t = vec_max<T>(chunk[min(v, n - 1)]);
+                  if (v < n) most[i] = fmaxf(most[i], t);  // each entry once only
+                }
+              uint32_t o[kAtOnce];
+#pragma unroll
+              for (int i = 0; i < kAtOnce; ++i) o[i] = order_bits(most[i]);
+              const uint32_t bits = kth_bits(o, k);
+              if (lane == 0 && bits > order_bits(-INFINITY)) atomicMax(&cut->key, (unsigned long long)bits << 32);
+              __syncwarp();
             }
-          uint32_t o[kAtOnce];
-#pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) o[i] = order_bits(most[i]);
-          const uint32_t bits = kth_bits(o, k);
-          if (lane == 0 && bits > order_bits(-INFINITY)) atomicMax(&cut->key, (unsigned long long)bits << 32);
-          __syncwarp();
-        }
-        const float value = cut_value<T>(*(volatile unsigned long long*)&cut->key);
-        uint32_t hits = 0;
+            const float value = cut_value<T>(*(volatile unsigned long long*)&cut->key);
+            uint32_t hits = 0;
 #pragma unroll 1
-        for (int r = 0; r < kRounds; ++r)
+            for (int r = 0; r < kRounds; ++r)
 #pragma unroll
-          for (int i = 0; i < kAtOnce; ++i) {
-            const int v = (r * kAtOnce + i) * 32 + lane;
-            hits |= (uint32_t)(reaches<T>(chunk[min(v, n - 1)], value) & (v < n)) << (r * kAtOnce + i);
-          }
-        n_cand = scan_hits<T>(reinterpret_cast<const T*>(chunk), hits, 32, 0, z.entry(v0), cand, n_cand, cut, k);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[slot]);
-        if ((seen & (seen - 1)) == 0) raise_cut<kScan * kCand>(&x.cand[b][0][0], cut, k);
-      });
+              for (int i = 0; i < kAtOnce; ++i) {
+                const int v = (r * kAtOnce + i) * 32 + lane;
+                hits |= (uint32_t)(reaches<T>(chunk[min(v, n - 1)], value) & (v < n)) << (r * kAtOnce + i);
+              }
+            n_cand = scan_hits<T>(reinterpret_cast<const T*>(chunk), hits, 32, 0, z.entry(v0), cand, n_cand, cut, k);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[slot]);
+            if ((seen & (seen - 1)) == 0) raise_cut<kScan * kCand>(&x.cand[b][0][0], cut, k);
+            return true;
+          }))
+        return;
     if (wid == 0 && rank == 0) {  // the edges
       const int j = lane < kEdges ? z.edge(lane) : -1;
       const float v = j >= 0 ? up(z.row[j]) : -INFINITY;
@@ -434,16 +488,16 @@ __device__ void scan_rows(Smem<kLogprobs>& sm, const Args& a, int rank, int wid,
 // The selecting warp: the best of a row's candidates, sorted.
 __device__ void select_rows(Smem<kLogprobs>& sm, const Args& a, int64_t row0, int64_t step) {
   const int lane = threadIdx.x & 31, k = a.t.k;
-  volatile int* ab = &sm.abort_flag;
+  Limit* limit = &sm.limit;
   ScanSmem& x = sm.x;
   int it = 0;
 #pragma unroll 1
   for (int64_t row = row0; row < a.r.rows; row += step, ++it) {
     const int b = it & 1;
     unsigned long long* cand = &x.cand[b][0][0];
-    wait(&sm.scanned[b], (it >> 1) & 1, ab);
+    if (!wait(&sm.scanned[b], (it >> 1) & 1, limit)) return;
     const int n = keep_best<kScan * kCand>(cand, *(volatile unsigned long long*)&x.cut[b].key, k);
-    if (it >= 1) wait(&sm.unlisted, (it - 1) & 1, ab);
+    if (it >= 1 && !wait(&sm.unlisted, (it - 1) & 1, limit)) return;
     rank_best(cand, n, k, [&](int at, unsigned long long key) { x.list[at] = key; });
     if (lane == 0) x.list_n = min(n, k);
     __syncwarp();
@@ -493,7 +547,7 @@ template <bool kEntropy, int kMode> __device__ __forceinline__ Sums row_sums(con
 template <typename T>
 __device__ void answer_rows(Smem<kLogprobs>& sm, const Args& a, int rank, int64_t row0, int64_t step) {
   const int lane = threadIdx.x & 31, C = a.C, k = a.t.k;
-  volatile int* ab = &sm.abort_flag;
+  Limit* limit = &sm.limit;
   ScanSmem& x = sm.x;
   int it = 0;
   if (lane < 2) mbar_arrive(&sm.ready[lane]);
@@ -512,10 +566,10 @@ __device__ void answer_rows(Smem<kLogprobs>& sm, const Args& a, int rank, int64_
       }
     }
     const Sums edges = lane_sums<true>(ze, je >= 0, a.c.hi);
-    wait(&sm.sums[b], ph, ab);
-    if (it >= 2) wait<true>(&sm.ack[b], ph ^ 1, ab);
+    if (!wait(&sm.sums[b], ph, limit)) return;
+    if (it >= 2 && !wait<true>(&sm.ack[b], ph ^ 1, limit)) return;
     if (k > 0) {
-      wait(&sm.listed, it & 1, ab);
+      if (!wait(&sm.listed, it & 1, limit)) return;
       const int n = x.list_n;
 #pragma unroll 1
       for (int o = 0; o < C; ++o)
@@ -530,7 +584,7 @@ __device__ void answer_rows(Smem<kLogprobs>& sm, const Args& a, int rank, int64_
       mbar_arrive(&sm.ready[b]);
       if (k > 0) mbar_arrive(&sm.unlisted);
     }
-    wait<true>(&sm.mail[b], ph, ab);
+    if (!wait<true>(&sm.mail[b], ph, limit)) return;
     const Sums p = row_sums<true>(sm, a, b);
     const Answer ans(p, a.c);
     if (k > 0) {
@@ -596,7 +650,7 @@ __device__ __forceinline__ void store_edges(const DistillRow& x, const Args& a, 
 template <typename T, int kMode>
 __device__ void teach_rows(Smem<kMode>& sm, const Args& a, int rank, int which, int64_t row0, int64_t step) {
   const int lane = threadIdx.x & 31;
-  volatile int* ab = &sm.abort_flag;
+  Limit* limit = &sm.limit;
   int it = which, idx[2];
   float lp[2];
   auto fetch = [&](int64_t row) {
@@ -618,7 +672,7 @@ __device__ void teach_rows(Smem<kMode>& sm, const Args& a, int rank, int which, 
     float zv[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) zv[h] = idx[h] >= 0 && idx[h] < z.n ? up(z.row[idx[h]]) : 0.f;
-    if (it >= Shape<kMode>::kBuf) wait(&sm.done[b], turn_of<kMode>(it) ^ 1, ab);
+    if (it >= Shape<kMode>::kBuf && !wait(&sm.done[b], turn_of<kMode>(it) ^ 1, limit)) return;
     DistillRow& x = sm.x[b];
     Teacher& t = x.t;
     load_teacher(t, sm.marks[which], a.d, idx, lp, zv, z.n, a.c);
@@ -668,7 +722,7 @@ __device__ void teach_rows(Smem<kMode>& sm, const Args& a, int rank, int which, 
 template <typename T, int kMode>
 __device__ void finish_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0, int64_t step) {
   const int lane = threadIdx.x & 31;
-  volatile int* ab = &sm.abort_flag;
+  Limit* limit = &sm.limit;
   int it = 0;
 #pragma unroll 1
   for (int64_t row = row0; row < a.r.rows; row += step, ++it) {
@@ -676,12 +730,12 @@ __device__ void finish_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t ro
     const Part<T> z(a, row, rank);
     DistillRow& x = sm.x[b];
     const float gr = kMode == kStep ? a.d.g[row] : 0.f;
-    wait(&sm.sums[b], ph, ab);
+    if (!wait(&sm.sums[b], ph, limit)) return;
     // Another block sends a row's part only after it has this block's part of the row before, which this warp sends
     // when it has read all of the row before that: so a place is read before it is written again. No other warp
     // reads the places; the writing warp, which may be some rows behind, has the joined sums.
     mail_sums<false>(sm, a, b, z.u0, z.u1, rank, x.edges);
-    wait<true>(&sm.mail[b], ph, ab);
+    if (!wait<true>(&sm.mail[b], ph, limit)) return;
     const Sums p = row_sums<false>(sm, a, b);
     if (lane == 0) x.joined = p;
     if constexpr (kMode == kStep) {
@@ -699,13 +753,13 @@ __device__ void finish_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t ro
 template <int kMode>
 __device__ void write_rows(Smem<kMode>& sm, const Args& a, int rank, int64_t row0, int64_t step) {
   const int lane = threadIdx.x & 31;
-  volatile int* ab = &sm.abort_flag;
+  Limit* limit = &sm.limit;
   int it = 0;
 #pragma unroll 1
   for (int64_t row = row0; row < a.r.rows; row += step, ++it) {
     const int b = buf_of<kMode>(it);
     const DistillRow& x = sm.x[b];
-    wait(&sm.joined[b], turn_of<kMode>(it), ab);
+    if (!wait(&sm.joined[b], turn_of<kMode>(it), limit)) return;
     if (rank == 0) store_loss(a.d, row, Student(x.joined, x.t, a.d, a.c), x.t, a.c);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.done[b]);
@@ -742,7 +796,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kBlocks)
     }
     tc::mbar_init(&sm.listed, 1);
     tc::mbar_init(&sm.unlisted, 1);
-    sm.abort_flag = 0;
+    sm.limit = Limit{a.wait_ns, 0};
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -759,7 +813,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kBlocks)
   pdl_wait();  // what the launch before this one wrote; nothing above touches it
   pdl_trigger();
   uint32_t row0, step;
-  asm volatile("mov.u32 %0, %%clusterid.x;\nmov.u32 %1, %%nclusterid.x;" : "=r"(row0), "=r"(step));
+  cluster_rows(row0, step);
   const int other = warp - S::kNW;
   if (other < 0) {
     sum_rows<T, kMode>(sm, a, rank, row0, step);
@@ -776,6 +830,7 @@ __global__ void __launch_bounds__(Shape<kMode>::kThreads, Shape<kMode>::kBlocks)
   }
   __syncwarp();
   cluster_sync();  // no block ends while another may write to it
+  if (sm.limit.over) give_up<T, kMode>(sm, a);
 }
 
 // ---- launches --------------------------------------------------------------------------------------
@@ -868,8 +923,11 @@ template <typename T, int kMode> cudaError_t run(const Args& args, cudaStream_t 
   return cudaLaunchKernelExC(&l.cfg, kernel, params);
 }
 
+thread_local unsigned long long wait_ns = tc::kTimeoutNs;
+
 Args args_of(const VocabRows& r) {
   Args a{};
+  a.wait_ns = wait_ns;
   a.r = r;
   a.c = scale_of(r.temperature);
   return a;
@@ -879,6 +937,8 @@ Args args_of(const VocabRows& r) {
 bool is_short(const VocabRows& r) { return (int64_t)r.vocab * (r.dtype == EAGLE_DTYPE_F32 ? 4 : 2) <= kShortRow; }
 
 }  // namespace
+
+void set_vocab_wait(int64_t ns) { wait_ns = ns < 0 ? tc::kTimeoutNs : (unsigned long long)ns; }
 
 cudaError_t token_logprobs(const VocabRows& r, const TokenLogprobs& t, cudaStream_t s) {
   Args a = args_of(r);

@@ -866,7 +866,32 @@ struct Args {
   Scale c;
   // long rows: blocks a row; units, whose sums are joined, of a row and of a block; vectors of a unit
   int C, units, mine, unit;
+  unsigned long long wait_ns;  // limit of a wait
 };
+
+// The results of a row of a call whose kernel gave up a wait: NaN (index -1), by `threads` threads.
+template <typename T, int kMode> __device__ __noinline__ void no_results(const Args& a, int64_t row, int thread, int threads) {
+  if constexpr (kMode == kLogprobs) {
+    if (thread == 0) {
+      if (a.t.logprob) a.t.logprob[row] = NAN;
+      if (a.t.entropy) a.t.entropy[row] = NAN;
+      if (a.t.lse) a.t.lse[row] = NAN;
+    }
+#pragma unroll 1
+    for (int i = thread; i < a.t.k; i += threads) {
+      a.t.idx[row * a.t.k + i] = -1;
+      a.t.val[row * a.t.k + i] = NAN;
+    }
+  } else {
+    if (kMode != kGrad && thread == 0) {
+      a.d.loss[row] = NAN;
+      for (int i = 0; a.d.stats && i < 4; ++i) a.d.stats[4 * row + i] = NAN;
+    }
+    if constexpr (kMode != kLoss)
+#pragma unroll 1
+      for (int64_t j = thread; j < a.r.vocab; j += threads) (reinterpret_cast<T*>(a.d.dz) + row * a.d.ld_dz)[j] = down<T>(NAN);
+  }
+}
 
 constexpr int kShortRow = 16 << 10;  // bytes of a row that one warp does by itself
 cudaError_t short_rows(const Args& a, int mode, cudaStream_t s);

@@ -46,4 +46,7 @@ cudaError_t distill_loss(const VocabRows& r, const Distill& d, cudaStream_t s);
 cudaError_t distill_grad(const VocabRows& r, const Distill& d, cudaStream_t s);
 cudaError_t distill_loss_grad(const VocabRows& r, const Distill& d, cudaStream_t s);
 
+// Limit of the kernels' waits in later calls from this host thread, for tests; below 0: 2 s as by default.
+void set_vocab_wait(int64_t ns);
+
 }  // namespace eg

@@ -32,13 +32,20 @@ struct alignas(16) WarpDistill {
 };
 template <int kMode> using WarpSmem = std::conditional_t<kMode == kLogprobs, WarpScan, WarpDistill>;
 
-// The copy's end; false if it does not come within 2 s (the row's results are missing then).
-__device__ bool wait_copy(uint64_t* bar) {
-  if (tc::mbar_try_wait(bar, 0)) return true;
-  const unsigned long long t0 = tc::globaltimer();
-  while (!tc::mbar_try_wait(bar, 0))
-    if (tc::globaltimer() - t0 > tc::kTimeoutNs) return false;
-  return true;
+// The copy's end, for the whole warp. False if it does not come within the limit (the row's results are NaN then);
+// a copy that is merely late still lands first (0.2 s more at most), as its place is the next block's afterwards.
+__device__ __forceinline__ bool wait_copy(uint64_t* bar, unsigned long long ns) {
+  bool ok = tc::mbar_try_wait(bar, 0);
+  if (!ok && ns > 0) {
+    const unsigned long long t0 = tc::globaltimer();
+    while (!(ok = tc::mbar_try_wait(bar, 0)) && tc::globaltimer() - t0 <= ns) {
+    }
+  }
+  if (__all_sync(kFull, ok)) return true;
+#pragma unroll 1
+  for (int tries = 0; tries < 100000 && !tc::mbar_try_wait(bar, 0); ++tries) {
+  }
+  return false;
 }
 
 template <typename T, bool kEntropy> __device__ __forceinline__ Sums sum_row(const uint4* v, int n, const Sums& edges, float c) {
@@ -117,7 +124,7 @@ __device__ void answer_row(WarpScan& x, const uint4* v, const Args& a, int64_t r
 }
 
 template <typename T, int kMode>
-__device__ void distill_row(WarpDistill& x, uint4* v, uint64_t* bar, const Args& a, int64_t row, const Row<T>& z, int je, float ze) {
+__device__ bool distill_row(WarpDistill& x, uint4* v, uint64_t* bar, const Args& a, int64_t row, const Row<T>& z, int je, float ze) {
   constexpr int kVec = El<T>::kVec;
   const int lane = threadIdx.x & 31;
   const Distill& d = a.d;
@@ -146,7 +153,7 @@ __device__ void distill_row(WarpDistill& x, uint4* v, uint64_t* bar, const Args&
     at[h] = x.t.idx[lane + 32 * h] - z.head;
     if (x.t.idx[lane + 32 * h] < 0 || at[h] >= z.nb * kVec) at[h] = -1;
   }
-  if (z.nb > 0 && !wait_copy(bar)) return;
+  if (z.nb > 0 && !wait_copy(bar, a.wait_ns)) return false;
   if constexpr (kMode == kGrad) {
     store_coef(x.k, d.stats + 4 * row, x.t, d, d.g[row], a.c);
   } else {
@@ -179,6 +186,7 @@ __device__ void distill_row(WarpDistill& x, uint4* v, uint64_t* bar, const Args&
       if (at[h] >= 0) out[at[h]] = down<T>(zero ? 0.f : x.k.g[lane + 32 * h]);
     if (je >= 0) dz[je] = down<T>(zero ? 0.f : listed >= 0 ? x.k.g[listed] : x.k.at(ze, a.c.hi));
   }
+  return true;
 }
 
 template <typename T, int kMode>
@@ -204,12 +212,14 @@ __global__ void __launch_bounds__(kWarps * 32) short_kernel(const __grid_constan
   __syncwarp();
   const int je = lane < kEdges ? z.edge(lane) : -1;
   const float ze = je >= 0 ? up(z.row[je]) : -INFINITY;
+  bool ok;
   if constexpr (kMode == kLogprobs) {
-    if (z.nb > 0 && !wait_copy(bar)) return;
-    answer_row<T>(x, v, a, row, z, je, ze);
+    ok = z.nb == 0 || wait_copy(bar, a.wait_ns);
+    if (ok) answer_row<T>(x, v, a, row, z, je, ze);
   } else {
-    distill_row<T, kMode>(x, v, bar, a, row, z, je, ze);
+    ok = distill_row<T, kMode>(x, v, bar, a, row, z, je, ze);
   }
+  if (!ok) no_results<T, kMode>(a, row, lane, 32);
 }
 
 template <typename T, int kMode> cudaError_t run_short(const Args& a, cudaStream_t s) {

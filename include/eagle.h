@@ -407,7 +407,9 @@ eagle_status eagle_op_tree_attention(int32_t dtype, int32_t rows, int32_t n_head
  * distribution; its results are NaN. rows = 0 is a call that does nothing. No
  * scratch: calls on different streams, and captured ones, never share memory that
  * the caller did not pass to both. The device current at the call must hold the
- * pointers. */
+ * pointers. There is no status word: where one of a kernel's bounded waits gives
+ * up (2 s), the call has still returned EAGLE_OK, and the results of every row of
+ * the blocks concerned are NaN (index -1), those that were right among them. */
 
 /* What a server answers with, per row: d_logprob [rows] = log q of the given token
  * d_tokens [rows] (both NULL: none wanted), 0 for a token of -1 (padding), NaN for
@@ -488,6 +490,11 @@ eagle_status eagle_set_trace(eagle_ctx* ctx, uint64_t* d_trace, size_t n, int32_
  * up, writes EAGLE_ERR_TIMEOUT to *d_status (if *d_status was EAGLE_OK) and the
  * kernel returns; no trap, no fault, and the CUDA context stays usable. */
 eagle_status eagle_selftest_bounded_wait(int32_t* d_status, void* stream);
+
+/* The same for the operators on vocabulary rows: their kernels' waits give up after
+ * ns nanoseconds (0: what is not there at the first look never is) in later calls
+ * from this host thread; below 0: after 2 s again. Returns EAGLE_OK. Host-only. */
+eagle_status eagle_selftest_vocab_wait(int64_t ns);
 
 #ifdef __cplusplus
 }
