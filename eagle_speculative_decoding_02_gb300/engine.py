@@ -424,12 +424,15 @@ def _teacher(logits, t_idx, t_logp, temperature, tail):
 
 
 def _grad_out(logits: torch.Tensor, rows: int, vocab: int, ld: int, out: torch.Tensor | None):
-    """The gradient's tensor and its row length. One made here has the logits' row length and offset from a
-    16-byte boundary, so that the kernel moves whole vectors."""
+    """The gradient's tensor and its row length. The rows of one made here start at the logits' offsets from 16-byte
+    boundaries, so that the kernel moves whole vectors, and lie as close as that allows, however far apart the
+    logits' are."""
     if out is None:
+        per = 16 // logits.element_size()
         skip = logits.data_ptr() % 16 // logits.element_size()
         if skip == 0 and ld == vocab:
             return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), ld
+        ld = vocab + (ld - vocab) % per
         flat = torch.empty(skip + rows * ld, dtype=logits.dtype, device=logits.device)
         out = flat.as_strided((rows, vocab), (ld, 1), skip)
         return (out if logits.dim() == 2 else out.unflatten(0, logits.shape[:-1]) if logits.dim() > 2 else out[0]), ld
