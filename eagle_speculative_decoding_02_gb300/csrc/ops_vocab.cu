@@ -27,6 +27,20 @@ bool apart(const void* z, int64_t ld, const void* dz, int64_t ld_dz, int32_t row
   return at >= row && ld * size - at >= row;
 }
 
+// Whether the gradient's rows leave an array (NULL: none) of `bytes` bytes alone; it may lie between them.
+bool clear_of(const void* dz, int64_t ld, int32_t rows, int32_t vocab, int size, const void* p, int64_t bytes) {
+  const int64_t at = (intptr_t)p - (intptr_t)dz, pitch = ld * size, row = (int64_t)vocab * size;
+  if (!p || at + bytes <= 0) return true;
+  const int64_t first = at < row ? 0 : (at - row) / pitch + 1;  // the first row that ends after the array begins
+  return first >= rows || first * pitch >= at + bytes;
+}
+
+bool grad_ok(int32_t rows, int32_t vocab, int size, const void* z, int64_t ld, const Distill& d) {
+  auto clear = [&](const void* p, int64_t each) { return clear_of(d.dz, d.ld_dz, rows, vocab, size, p, rows * each); };
+  return d.g && matrix_ok(d.dz, size, rows, vocab, d.ld_dz) && apart(z, ld, d.dz, d.ld_dz, rows, vocab, size) &&
+         clear(d.t_idx, 4 * d.k) && clear(d.t_lp, 4 * d.k) && clear(d.g, 4) && clear(d.stats, 16) && clear(d.loss, 4);
+}
+
 bool rows_ok(int32_t dtype, int32_t rows, int32_t vocab, int64_t ld, const void* z, float temperature) {
   return esize(dtype) && rows >= 0 && vocab >= 1 && temperature >= 1e-6f && temperature <= 1e6f &&
          (rows == 0 || matrix_ok(z, esize(dtype), rows, vocab, ld));
@@ -83,11 +97,9 @@ eagle_status eagle_op_distill_grad(int32_t dtype, int32_t rows, int32_t vocab, i
   if (!rows_ok(dtype, rows, vocab, ld, d_logits, temperature) || !teacher_ok(rows, k, d_t_idx, d_t_logp, tail))
     return EAGLE_ERR_INVALID_ARG;
   if (rows == 0) return EAGLE_OK;
-  if (!d_stats || !d_g || !matrix_ok(d_dlogits, esize(dtype), rows, vocab, ld_out) ||
-      !apart(d_logits, ld, d_dlogits, ld_out, rows, vocab, esize(dtype)))
-    return EAGLE_ERR_INVALID_ARG;
   const VocabRows r{d_logits, dtype, rows, vocab, ld, temperature};
   const Distill d{k, d_t_idx, d_t_logp, tail, nullptr, const_cast<float*>(d_stats), d_g, d_dlogits, ld_out};
+  if (!d_stats || !grad_ok(rows, vocab, esize(dtype), d_logits, ld, d)) return EAGLE_ERR_INVALID_ARG;
   return launched([&] { return distill_grad(r, d, (cudaStream_t)stream); });
 }
 
@@ -98,12 +110,11 @@ eagle_status eagle_op_distill_loss_grad(int32_t dtype, int32_t rows, int32_t voc
   if (!rows_ok(dtype, rows, vocab, ld, d_logits, temperature) || !teacher_ok(rows, k, d_t_idx, d_t_logp, tail))
     return EAGLE_ERR_INVALID_ARG;
   if (rows == 0) return EAGLE_OK;
-  if (!d_loss || (!d_stats && (int64_t)vocab * esize(dtype) > EAGLE_DISTILL_ONE_PASS_BYTES) || !d_g ||
-      !matrix_ok(d_dlogits, esize(dtype), rows, vocab, ld_out) ||
-      !apart(d_logits, ld, d_dlogits, ld_out, rows, vocab, esize(dtype)))
-    return EAGLE_ERR_INVALID_ARG;
   const VocabRows r{d_logits, dtype, rows, vocab, ld, temperature};
   const Distill d{k, d_t_idx, d_t_logp, tail, d_loss, d_stats, d_g, d_dlogits, ld_out};
+  if (!d_loss || (!d_stats && (int64_t)vocab * esize(dtype) > EAGLE_DISTILL_ONE_PASS_BYTES) ||
+      !grad_ok(rows, vocab, esize(dtype), d_logits, ld, d))
+    return EAGLE_ERR_INVALID_ARG;
   return launched([&] { return distill_loss_grad(r, d, (cudaStream_t)stream); });
 }
 

@@ -115,3 +115,17 @@ def test_binding_refuses_host_tensors_and_types():
         op_token_logprobs(torch.zeros(2, 8, dtype=torch.float64))
     with pytest.raises(ValueError):
         op_distill_loss(torch.zeros(2, 8), torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1))
+
+
+# the gradient's rows (of 400 bytes, from 2 P on; with ld_out = 200 every 800 bytes) and another array of the call
+MEETS = [(f, o) for f in ("eagle_op_distill_grad", "eagle_op_distill_loss_grad") for o in
+         [dict(idx=2 * P), dict(idx=2 * P + 1596), dict(idx=2 * P - 76), dict(lp=2 * P + 400), dict(lp=2 * P - 4, ld_out=200),
+          dict(g=2 * P - 12), dict(g=2 * P + 1596), dict(g=2 * P + 1600 + 396, ld_out=200), dict(g=2 * P + 796, ld_out=200),
+          dict(stats=2 * P - 60), dict(stats=2 * P + 1200), dict(stats=2 * P + 2400 - 60, ld_out=200),
+          dict(k=64, idx=2 * P - 1020), dict(dtype=1, ld_out=101, idx=2 * P + 200 + 204 * 2)]]
+MEETS += [("eagle_op_distill_loss_grad", o) for o in [dict(loss=2 * P), dict(loss=2 * P - 12), dict(loss=2 * P + 1596)]]
+
+
+@pytest.mark.parametrize("fn,over", MEETS)
+def test_gradients_over_other_arguments_are_refused(lib, fn, over):
+    assert getattr(lib, fn)(*{**GOOD[fn], **over}.values()) == 1
