@@ -11,6 +11,9 @@ int esize(int dtype) {
   return dtype == EAGLE_DTYPE_F32 ? 4 : dtype == EAGLE_DTYPE_BF16 || dtype == EAGLE_DTYPE_F16 ? 2 : 0;
 }
 
+// Arrays of 4-byte elements, aligned to them (NULL is).
+template <typename... P> bool words_ok(const P*... p) { return (((uintptr_t)p % 4 == 0) && ...); }
+
 // A row-major matrix of `size`-byte elements: aligned to them, rows that do not overlap.
 bool matrix_ok(const void* p, int size, int32_t rows, int32_t vocab, int64_t ld) {
   return p && (uintptr_t)p % size == 0 && ld >= vocab && ld <= INT64_MAX / 8 / rows;
@@ -37,7 +40,7 @@ bool clear_of(const void* dz, int64_t ld, int32_t rows, int32_t vocab, int size,
 
 bool grad_ok(int32_t rows, int32_t vocab, int size, const void* z, int64_t ld, const Distill& d) {
   auto clear = [&](const void* p, int64_t each) { return clear_of(d.dz, d.ld_dz, rows, vocab, size, p, rows * each); };
-  return d.g && matrix_ok(d.dz, size, rows, vocab, d.ld_dz) && apart(z, ld, d.dz, d.ld_dz, rows, vocab, size) &&
+  return d.g && words_ok(d.g, d.stats, d.loss) && matrix_ok(d.dz, size, rows, vocab, d.ld_dz) && apart(z, ld, d.dz, d.ld_dz, rows, vocab, size) &&
          clear(d.t_idx, 4 * d.k) && clear(d.t_lp, 4 * d.k) && clear(d.g, 4) && clear(d.stats, 16) && clear(d.loss, 4);
 }
 
@@ -47,7 +50,7 @@ bool rows_ok(int32_t dtype, int32_t rows, int32_t vocab, int64_t ld, const void*
 }
 
 bool teacher_ok(int32_t rows, int32_t k, const int32_t* idx, const float* lp, int32_t tail) {
-  return k >= 1 && k <= EAGLE_MAX_TEACHER && (tail == 0 || tail == 1) && (rows == 0 || (idx && lp));
+  return k >= 1 && k <= EAGLE_MAX_TEACHER && (tail == 0 || tail == 1) && (rows == 0 || (idx && lp && words_ok(idx, lp)));
 }
 
 // What a launch says; nothing is thrown through the C entry points.
@@ -72,7 +75,8 @@ eagle_status eagle_op_token_logprobs(int32_t dtype, int32_t rows, int32_t vocab,
       !d_tokens != !d_logprob)
     return EAGLE_ERR_INVALID_ARG;
   if (rows == 0) return EAGLE_OK;
-  if (k > 0 && (!d_idx || !d_val)) return EAGLE_ERR_INVALID_ARG;
+  if ((k > 0 && (!d_idx || !d_val)) || !words_ok(d_tokens, d_logprob, d_entropy, d_lse, d_idx, d_val))
+    return EAGLE_ERR_INVALID_ARG;
   const VocabRows r{d_logits, dtype, rows, vocab, ld, temperature};
   const TokenLogprobs t{d_tokens, k, d_logprob, d_entropy, d_lse, d_idx, d_val};
   return launched([&] { return token_logprobs(r, t, (cudaStream_t)stream); });
@@ -84,7 +88,7 @@ eagle_status eagle_op_distill_loss(int32_t dtype, int32_t rows, int32_t vocab, i
   if (!rows_ok(dtype, rows, vocab, ld, d_logits, temperature) || !teacher_ok(rows, k, d_t_idx, d_t_logp, tail))
     return EAGLE_ERR_INVALID_ARG;
   if (rows == 0) return EAGLE_OK;
-  if (!d_loss || !d_stats) return EAGLE_ERR_INVALID_ARG;
+  if (!d_loss || !d_stats || !words_ok(d_loss, d_stats)) return EAGLE_ERR_INVALID_ARG;
   const VocabRows r{d_logits, dtype, rows, vocab, ld, temperature};
   const Distill d{k, d_t_idx, d_t_logp, tail, d_loss, d_stats, nullptr, nullptr, 0};
   return launched([&] { return distill_loss(r, d, (cudaStream_t)stream); });

@@ -398,10 +398,10 @@ eagle_status eagle_op_tree_attention(int32_t dtype, int32_t rows, int32_t n_head
                                      size_t scratch_bytes, void* stream);
 
 /* ---- Operators on vocabulary rows -------------------------------------------
- * Logits d_logits [rows][ld] of dtype float32, bfloat16 or half (element-aligned,
- * any row length ld >= vocab; entries vocab..ld-1 of a row are neither read nor
- * written), for example the logits of eagle_verify. q = softmax(logits /
- * temperature) of a row, temperature in [1e-6, 1e6]. Sums, logarithms and results
+ * Logits d_logits [rows][ld] of dtype float32, bfloat16 or half (any row length
+ * ld >= vocab; entries vocab..ld-1 of a row are neither read nor written). Every
+ * array starts at a multiple of its element's size. q = softmax(logits /
+ * temperature) of a row of logits, for example eagle_verify's, temperature in [1e-6, 1e6]. Sums, logarithms and results
  * are float32 or wider whatever the logits' type. An entry of -inf has
  * probability 0. A row that holds a NaN or +inf, or nothing but -inf, has no
  * distribution; its results are NaN. rows = 0 is a call that does nothing. No

@@ -129,3 +129,15 @@ MEETS += [("eagle_op_distill_loss_grad", o) for o in [dict(loss=2 * P), dict(los
 @pytest.mark.parametrize("fn,over", MEETS)
 def test_gradients_over_other_arguments_are_refused(lib, fn, over):
     assert getattr(lib, fn)(*{**GOOD[fn], **over}.values()) == 1
+
+
+ODD = [("eagle_op_token_logprobs", n) for n in ("tok", "lp", "ent", "lse", "idx", "val")] + \
+    [("eagle_op_distill_loss", n) for n in ("idx", "lp", "loss", "stats")] + \
+    [("eagle_op_distill_grad", n) for n in ("idx", "lp", "stats", "g")] + \
+    [("eagle_op_distill_loss_grad", n) for n in ("idx", "lp", "g", "loss", "stats")]
+
+
+@pytest.mark.parametrize("fn,name", ODD)
+def test_arrays_off_their_elements_size_are_refused(lib, fn, name):
+    for off in (1, 2, 3):
+        assert getattr(lib, fn)(*{**GOOD[fn], name: P + off}.values()) == 1
