@@ -21,7 +21,7 @@ bool matrix_ok(const void* p, int size, int32_t rows, int32_t vocab, int64_t ld)
 
 // The gradient may take the logits' place; otherwise no row of one may reach into a row of the other.
 bool apart(const void* z, int64_t ld, const void* dz, int64_t ld_dz, int32_t rows, int32_t vocab, int size) {
-  if (z == dz && ld == ld_dz) return true;
+  if (z == dz && (ld == ld_dz || rows == 1)) return true;
   const int64_t diff = (intptr_t)dz - (intptr_t)z;  // bytes
   const int64_t row = (int64_t)vocab * size;
   if (diff >= (rows - 1) * ld * size + row || -diff >= (rows - 1) * ld_dz * size + row) return true;

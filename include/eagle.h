@@ -455,8 +455,9 @@ eagle_status eagle_op_distill_loss(int32_t dtype, int32_t rows, int32_t vocab, i
  * d_g [rows] the gradient of whatever is trained with respect to each row's loss (a
  * row whose d_g is 0 gets zeros). d_stats from eagle_op_distill_loss on the same
  * logits, teacher, temperature and tail. d_dlogits may be d_logits itself (with
- * ld_out = ld); rows that overlap in any other way are refused, and so are ones
- * that overlap the teacher, d_stats, d_g or d_loss. Rows that start at
+ * ld_out = ld, if there are several rows); rows that overlap in any other way are
+ * refused, and so are ones that overlap the teacher, d_stats, d_g or d_loss, or
+ * that lie between the logits' rows at another distance. Rows that start at
  * the same offset from a 16-byte boundary in both are fastest. */
 eagle_status eagle_op_distill_grad(int32_t dtype, int32_t rows, int32_t vocab, int64_t ld, const void* d_logits,
                                    int32_t k, const int32_t* d_t_idx, const float* d_t_logp, float temperature,
