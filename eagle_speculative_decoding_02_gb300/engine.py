@@ -334,6 +334,7 @@ def op_tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: t
 
 
 _VOCAB_DTYPES = {torch.float32: L.DTYPE_F32, torch.bfloat16: L.DTYPE_BF16, torch.float16: L.DTYPE_F16}
+_MOST = 2 ** 31 - 1     # rows and entries of a row, 32 bits in the C calls
 
 
 def _vocab_rows(t: torch.Tensor, name: str = "logits") -> tuple[int, int, int]:
@@ -351,6 +352,8 @@ def _vocab_rows(t: torch.Tensor, name: str = "logits") -> tuple[int, int, int]:
             ld = vocab
         elif ld < vocab:
             raise ValueError(f"{name}: rows overlap in memory")
+        if rows > _MOST or vocab > _MOST:   # ctypes would take them modulo 2^32
+            raise ValueError(f"{name}: {rows} rows of {vocab}, more than {_MOST}")
         return rows, vocab, ld
     if t.dim() == 0:
         raise ValueError(f"{name} must have a vocabulary dimension")
@@ -402,11 +405,13 @@ def op_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     rows, vocab, ld = _vocab_rows(logits)
     dev, on, lead = logits.get_device(), logits.device, logits.shape[:-1]
     tok = _vocab_arg(tokens, "tokens", torch.int32, lead, dev) if tokens is not None else None
+    if not 0 <= k <= L.MAX_ALTERNATIVES:
+        L.check("eagle_op_token_logprobs", 1)
     lp = torch.empty(lead, dtype=torch.float32, device=on) if tok is not None else None
     entropy = torch.empty(lead, dtype=torch.float32, device=on)
     lse = torch.empty(lead, dtype=torch.float32, device=on)
-    idx = torch.empty((*lead, max(k, 0)), dtype=torch.int32, device=on)
-    val = torch.empty((*lead, max(k, 0)), dtype=torch.float32, device=on)
+    idx = torch.empty((*lead, k), dtype=torch.int32, device=on)
+    val = torch.empty((*lead, k), dtype=torch.float32, device=on)
     _vocab_call("eagle_op_token_logprobs", dev, _VOCAB_DTYPES[logits.dtype], rows, vocab, ld, logits.data_ptr(), tok,
                 temperature, k, lp.data_ptr() if lp is not None else None, entropy.data_ptr(), lse.data_ptr(),
                 idx.data_ptr(), val.data_ptr())
@@ -418,7 +423,7 @@ def _teacher(logits, t_idx, t_logp, temperature, tail):
     rows, vocab, ld = _vocab_rows(logits)
     dev, k = logits.get_device(), t_idx.shape[-1] if t_idx.dim() else 0
     shape = (*logits.shape[:-1], k)
-    return (_VOCAB_DTYPES[logits.dtype], rows, vocab, ld, logits.data_ptr(), k,
+    return (_VOCAB_DTYPES[logits.dtype], rows, vocab, ld, logits.data_ptr(), min(k, L.MAX_TEACHER + 1),
             _vocab_arg(t_idx, "t_idx", torch.int32, shape, dev),
             _vocab_arg(t_logp, "t_logp", torch.float32, shape, dev), temperature, 1 if tail else 0)
 
