@@ -446,6 +446,12 @@ def _grad_out(logits: torch.Tensor, rows: int, vocab: int, ld: int, out: torch.T
     return out, _vocab_rows(out, "out")[2]
 
 
+def _overwritten(t: torch.Tensor) -> None:
+    """So that autograd graphs that saved the tensor refuse to use it."""
+    if not t.is_inference():    # which has no version
+        torch.autograd.graph.increment_version(t)
+
+
 def op_distill_loss(logits: torch.Tensor, t_idx: torch.Tensor, t_logp: torch.Tensor, *, temperature: float = 1.0,
                     tail: bool = True):
     """Distillation of a student's logits [..., vocab] from a teacher's k best tokens per row, t_idx [..., k]
@@ -455,6 +461,8 @@ def op_distill_loss(logits: torch.Tensor, t_idx: torch.Tensor, t_logp: torch.Ten
     loss = KL(teacher || softmax(logits / temperature)) over the listed tokens and, with tail, "any other
     token" as one more outcome; without it the teacher's k tokens are renormalised. stats carries the sums to
     op_distill_grad. A row without an entry is padding (loss 0); indices outside the vocabulary give NaN.
+    The op_distill_* are no part of an autograd graph: what they return needs no gradient, and the gradient they give
+    is passed on by the caller (logits.backward(gradient), or a torch.autograd.Function around the pair).
     """
     args = _teacher(logits, t_idx, t_logp, temperature, tail)
     lead = logits.shape[:-1]
@@ -468,14 +476,17 @@ def op_distill_grad(logits: torch.Tensor, t_idx: torch.Tensor, t_logp: torch.Ten
                     grad: torch.Tensor, *, temperature: float = 1.0, tail: bool = True,
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """The gradient of op_distill_loss with respect to the logits, times each row's grad [...] (float32), in
-    the logits' type; stats from op_distill_loss with the same arguments. out may be the logits themselves."""
+    the logits' type; stats from op_distill_loss with the same arguments. out may be the logits themselves (an
+    overwritten tensor's version counts up, as after torch's own in-place operations)."""
     args = _teacher(logits, t_idx, t_logp, temperature, tail)
     dev, lead = logits.get_device(), logits.shape[:-1]
     st = _vocab_arg(stats, "stats", torch.float32, (*lead, 4), dev)
     g = _vocab_arg(grad, "grad", torch.float32, lead, dev)
-    out, ld_out = _grad_out(logits, *args[1:4], out)
-    _vocab_call("eagle_op_distill_grad", dev, *args, st, g, ld_out, out.data_ptr())
-    return out
+    dz, ld_out = _grad_out(logits, *args[1:4], out)
+    _vocab_call("eagle_op_distill_grad", dev, *args, st, g, ld_out, dz.data_ptr())
+    if out is not None:
+        _overwritten(out)
+    return dz
 
 
 def op_distill_loss_grad(logits: torch.Tensor, t_idx: torch.Tensor, t_logp: torch.Tensor, grad: torch.Tensor, *,
@@ -485,11 +496,13 @@ def op_distill_loss_grad(logits: torch.Tensor, t_idx: torch.Tensor, t_logp: torc
     args = _teacher(logits, t_idx, t_logp, temperature, tail)
     dev, lead = logits.get_device(), logits.shape[:-1]
     g = _vocab_arg(grad, "grad", torch.float32, lead, dev)
-    out, ld_out = _grad_out(logits, *args[1:4], out)
+    dz, ld_out = _grad_out(logits, *args[1:4], out)
     loss = torch.empty(lead, dtype=torch.float32, device=logits.device)
     stats = None    # between the two passes over longer rows
     if args[2] * logits.element_size() > L.DISTILL_ONE_PASS_BYTES:
         stats = torch.empty((*lead, 4), dtype=torch.float32, device=logits.device)
     _vocab_call("eagle_op_distill_loss_grad", dev, *args, g, loss.data_ptr(),
-                stats.data_ptr() if stats is not None else None, ld_out, out.data_ptr())
-    return loss, out
+                stats.data_ptr() if stats is not None else None, ld_out, dz.data_ptr())
+    if out is not None:
+        _overwritten(out)
+    return loss, dz
