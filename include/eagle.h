@@ -431,7 +431,9 @@ eagle_status eagle_op_token_logprobs(int32_t dtype, int32_t rows, int32_t vocab,
  *     max(0, 1 - sum p_i) for the teacher and q_t = the sum of q over the unlisted
  *     tokens for the student; where the student has no other token left (none is
  *     unlisted, or every unlisted logit is -inf or over 1e30 temperature below the
- *     row's largest, as masks of the type's lowest value are) p_t counts as 0;
+ *     row's largest, as masks of float32's or bfloat16's lowest value are) p_t
+ *     counts as 0. Half's lowest value, -65504, is a logit like any other: entries
+ *     masked with it keep p_t, at a loss of some 65504 p_t; mask half with -inf;
  *   tail = 0: p = softmax(d_t_logp) over the listed tokens (any common offset
  *     cancels), p_t = 0.
  *   d_loss[row] = sum p_i (log p_i - log q_i) + p_t (log p_t - log q_t)
