@@ -443,7 +443,7 @@ eagle_status eagle_op_token_logprobs(int32_t dtype, int32_t rows, int32_t vocab,
  * given twice counts once, with its first log probability; terms with p = 0 are 0.
  * A row with no entry is padding: loss and gradient 0, whatever its logits hold. A
  * row with any other index outside [0, vocab), or a log probability that is NaN or
- * +inf (tail = 1: whose exponential overflows), has loss and gradient NaN. So has,
+ * +inf (tail = 1: whose exponential overflows float32, or the row's sum of them), has loss and gradient NaN. So has,
  * with a teacher, a row whose student has no distribution.
  * d_stats [rows][4] carries the sums from the loss to the gradient: the largest
  * logit m and log sum exp((logit - m) / temperature); the same two over the unlisted

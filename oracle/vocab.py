@@ -44,7 +44,7 @@ def _teacher(t_idx, t_logp, vocab, tail):
         return None
     if tail:
         pr = np.exp(lp)
-        return idx, pr, max(0.0, 1.0 - pr.sum())
+        return (idx, pr, max(0.0, 1.0 - pr.sum())) if pr.sum() <= np.finfo(np.float32).max else None
     if not len(lp) or lp.max() == -np.inf:
         return idx, np.zeros(len(lp)), 0.0
     pr = np.exp(lp - lp.max())

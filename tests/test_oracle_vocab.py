@@ -141,3 +141,11 @@ ODD = [("eagle_op_token_logprobs", n) for n in ("tok", "lp", "ent", "lse", "idx"
 def test_arrays_off_their_elements_size_are_refused(lib, fn, name):
     for off in (1, 2, 3):
         assert getattr(lib, fn)(*{**GOOD[fn], name: P + off}.values()) == 1
+
+
+def test_teachers_whose_sum_overflows_are_broken():
+    """Each exponential fits float32, their sum does not; a twice given token counts once."""
+    z = np.zeros(9)
+    assert np.isnan(OV.distill(z, [1, 2], [88.5, 88.5])[0]) and np.isnan(OV.distill(z, [1, 2], [88.5, 88.5])[2]).all()
+    assert np.isfinite(OV.distill(z, [1, 1], [88.5, 88.5])[0]) and np.isfinite(OV.distill(z, [1, 2], [88.5, 80.0])[0])
+    assert np.isfinite(OV.distill(z, [1, 2], [88.5, 88.5], tail=False)[0])
