@@ -26,16 +26,18 @@
 //
 // Measured on one GB300 (128256 entries of bf16; passes replayed from a graph; copy
 // bandwidth 6.78 TB/s):
-//   loss, 1024 rows           45.1 us = 5.8 TB/s; the first row waits for its teacher, and
+//   loss, 1024 rows           45.7 us = 5.7 TB/s; the first row waits for its teacher, and
 //                             the last round has 112 rows for 152 blocks
-//   gradient, 1024 rows       88 us = 6.0 TB/s, bound by the memory
-//   step, 2048 rows, k = 64   183 us = 5.7 TB/s read and written; clusters of 4 fill 144 of
+//   gradient, 1024 rows       89 us = 5.9 TB/s, bound by the memory
+//   step, 2048 rows, k = 64   184 us = 5.7 TB/s read and written; clusters of 4 fill 144 of
 //                             152 SMs (of 8, as float32 rows need, 120); then the summing
 //                             warps' instructions (60% of the issue slots, ALU pipe 44%)
-//   log probabilities, 2048 rows, k = 16: 126.4 us = 4.2 TB/s (without alternatives, 1024
-//                             rows, 49 us = 5.4): instructions, 68% of the issue slots on 30
-//                             warps; the scan's second look at each vector and the entropy's
-//                             second sum are what it has beyond the loss
+//   log probabilities, 2048 rows, k = 16: 127 us = 4.1 TB/s (k = 64: 222; without
+//                             alternatives, 1024 rows, 49.5 us = 5.3): instructions, 68% of the
+//                             issue slots on 30 warps; the scan's second look at each vector and
+//                             the entropy's second sum are what it has beyond the loss
+//   waits that say whether they were met, which a role leaves its rows on if not, cost a
+//                             step 1% (183.7 to 185.8 us in turn), the rest less
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -872,14 +874,18 @@ template <typename T, int kMode> int max_clusters(int C, size_t smem) {
 //  - for log probabilities a row has up to 4 units, and up to 4 blocks: the count whose
 //    rounds over the rows take least, a block's part of a row costing its bytes and
 //    kRowBytes more for its ends, which are not overlapped in full (kListBytes where there
-//    are alternatives): 1024 rows of 128256 bf16 entries take 137 us with one block a row and
-//    155 with two at k = 64, without alternatives 54 and 49; 61 rows of float32 at k = 10
-//    take 22.7, 16.5 and 14.4 us with 1, 2 and 4;
+//    are alternatives): 1024 rows of 128256 bf16 entries take 132 us with one block a row and
+//    151 with two at k = 64, without alternatives 54 and 49; 61 rows of float32 at k = 10
+//    take 20.9, 15.3 and 14.0 us with 1, 2 and 4;
 //  - for a loss a unit is a block's part, and their number follows from the length: the
-//    least that keeps a part within kLossPart bytes (1024 rows of bf16: 45.7 us with one or
-//    two blocks, 59 with four), or, in a step, two parts in the ring (with two chunks of
-//    room where the cluster allows it: 182 us for 2048 rows with four, 289 with eight);
-//  - the gradient alone has no sums: as for log probabilities (1024 rows of bf16 86, 88
+//    least that keeps a part within kLossPart bytes, or, in a step, two parts in the ring (with
+//    two chunks of room where the cluster allows it: 184 us for 2048 rows with four, 289 with
+//    eight). Where kLossPart lies within 200 to 500 KB matters little with many rows (1024
+//    rows of 250 KB: 45.7 us with one block, 44.7 with two; 600 of 400 KB: 41.5 and 42.6; 500
+//    of 500 KB: 45.1, 43.7), while smaller parts cost more (four blocks 55.3, 47.7, 42.4; eight
+//    108, 72, 57) and few rows of 250 KB would gain (30 rows: 9.7 us with one block, 7.8 with
+//    two, 7.1 with four), which a count that follows from the length alone cannot have;
+//  - the gradient alone has no sums: as for log probabilities (1024 rows of bf16 87, 89
 //    and 90 us with 1, 2 and 4).
 constexpr int64_t kRowBytes = 24 << 10, kListBytes = 96 << 10, kLossPart = 264 << 10;
 

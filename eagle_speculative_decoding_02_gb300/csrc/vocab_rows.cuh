@@ -132,7 +132,8 @@ __device__ __forceinline__ float exp_scaled(float d, const Scale& c) {
 }
 
 // A number as the sum of two floats, for the last steps of a row, where differences
-// of logarithms of some 10 in size have to be good to 2^-24 of a result near 0.
+// of logarithms of some 10 in size have to be good to 2^-24 of a result near 0. Sums by
+// Knuth's two-sum, products by a fused multiply-add's rest.
 // (float64 would do, at a 64th of float32's rate on this GPU.) Where h is infinite l
 // may be NaN: value() takes h alone then.
 struct Two {
@@ -470,7 +471,8 @@ template <int kN> __device__ __noinline__ void raise_cut(const unsigned long lon
   if (lane == 0) atomicMax(&cut->key, (unsigned long long)bits << 32);
 }
 
-// Whether a vector has an entry that reaches `value` (one of the type's).
+// Whether a vector has an entry that reaches `value`, any float: rounded to the type, up or down, it passes over no
+// entry that does (rounded up, it is the least of the type's numbers above it), and scan_hits compares keys exactly.
 template <typename T> __device__ __forceinline__ bool reaches(const uint4& q, float value);
 template <> __device__ __forceinline__ bool reaches<float>(const uint4& q, float value) { return vec_max<float>(q) >= value; }
 template <> __device__ __forceinline__ bool reaches<bf16>(const uint4& q, float value) {

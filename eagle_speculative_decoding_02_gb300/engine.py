@@ -184,7 +184,8 @@ class EagleEngine:
     def verify_logprobs(self, tree: Tree, k: int = 0, temperature: float = 1.0):
         """verify, with what a server answers about each tree row's next token (op_token_logprobs of the target's
         logits): (choice, logprob of the choice, entropy, idx, val), idx and val [B, n_rows, k] the k most likely
-        tokens and their log probabilities."""
+        tokens and their log probabilities. Rows whose tree.tokens is -1 (the padding of a sequence with fewer nodes)
+        hold numbers that mean nothing."""
         am, lg = self.verify(tree, logits=True)
         lp, entropy, _, idx, val = op_token_logprobs(lg, am, k, temperature=temperature)
         return am, lp, entropy, idx, val

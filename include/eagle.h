@@ -236,7 +236,9 @@ eagle_status eagle_draft_tree(eagle_ctx* ctx, eagle_tree* out);
  * forward pass): target pass over tree->n_rows rows per sequence at positions
  * L + depth, K/V written to slots L + row. d_argmax [batch][n_rows] receives the
  * greedy token after each row; d_logits [batch][n_rows][vocab] float32 receives
- * the logits when not NULL (debug/parity path). The tree may be the one
+ * the logits when not NULL (for eagle_op_token_logprobs, or a user's own rule; the
+ * step itself does not store them). What both hold for padding rows (token -1) means
+ * nothing. The tree may be the one
  * eagle_draft_tree returned or any caller-built tree (n_rows <= 121). The tree
  * is checked on the device against the rules stated at eagle_tree: a tree
  * that breaks one sets the device status, nothing is committed by the
@@ -401,13 +403,13 @@ eagle_status eagle_op_tree_attention(int32_t dtype, int32_t rows, int32_t n_head
  * Logits d_logits [rows][ld] of dtype float32, bfloat16 or half (any row length
  * ld >= vocab; entries vocab..ld-1 of a row are neither read nor written). Every
  * array starts at a multiple of its element's size. q = softmax(logits /
- * temperature) of a row of logits, for example eagle_verify's, temperature in [1e-6, 1e6]. Sums, logarithms and results
- * are float32 or wider whatever the logits' type. An entry of -inf has
- * probability 0. A row that holds a NaN or +inf, or nothing but -inf, has no
- * distribution; its results are NaN. rows = 0 is a call that does nothing. No
- * scratch: calls on different streams, and captured ones, never share memory that
- * the caller did not pass to both. The device current at the call must hold the
- * pointers. There is no status word: where one of a kernel's bounded waits gives
+ * temperature) of a row of logits, for example eagle_verify's, temperature in
+ * [1e-6, 1e6]. Sums, logarithms and results are float32 or wider whatever the
+ * logits' type. An entry of -inf has probability 0. A row that holds a NaN or +inf,
+ * or nothing but -inf, has no distribution; its results are NaN. rows = 0 is a call
+ * that does nothing. No scratch: calls on different streams, and captured ones,
+ * never share memory that the caller did not pass to both. The device current at
+ * the call must hold the pointers. There is no status word: where one of a kernel's bounded waits gives
  * up (2 s), the call has still returned EAGLE_OK, and the results of every row of
  * the blocks concerned are NaN (index -1), those that were right among them. */
 
@@ -443,8 +445,9 @@ eagle_status eagle_op_token_logprobs(int32_t dtype, int32_t rows, int32_t vocab,
  * given twice counts once, with its first log probability; terms with p = 0 are 0.
  * A row with no entry is padding: loss and gradient 0, whatever its logits hold. A
  * row with any other index outside [0, vocab), or a log probability that is NaN or
- * +inf (tail = 1: whose exponential overflows float32, or the row's sum of them), has loss and gradient NaN. So has,
- * with a teacher, a row whose student has no distribution.
+ * +inf (tail = 1: whose exponential overflows float32, or the row's sum of them),
+ * has loss and gradient NaN. So has, with a teacher, a row whose student has no
+ * distribution.
  * d_stats [rows][4] carries the sums from the loss to the gradient: the largest
  * logit m and log sum exp((logit - m) / temperature); the same two over the unlisted
  * tokens alone, m_t and its sum (tail = 1: -inf and 0 where p_t counts as 0; tail =
